@@ -76,23 +76,26 @@ __device__ __forceinline__ u32x2 ldtr(const lds_u8* p) {
 
 // Direct load of 16 bytes per lane into LDS at lds + 16 * lane (lds wave-uniform). The compiler
 // keeps no account of it: the kernels wait for it (wait_vmem_all and a barrier) before the buffer
-// is read, and issue none into a buffer before a barrier has ended every read of it.
+// is read, and issue none into a buffer before a barrier has ended every read of it. Nor does it put
+// wait states into the assembly: one stands between the write of M0 and the load that takes its base
+// from it.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
                "s"(__builtin_amdgcn_readfirstlane(lds))
                : "memory", "m0");
 }
 #pragma clang diagnostic pop
-// The same from the wave-uniform address `src` plus a 32-bit byte offset a lane.
+// The same from the wave-uniform address `src` plus a 32-bit byte offset a lane. With M0's write, five
+// wait states after what may be a v_readfirstlane of the address.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void* src, uint32_t off, uint32_t lds) {
   const uint64_t at = (uint64_t)src;
   const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32)) << 32 |
                         (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
                "s"(__builtin_amdgcn_readfirstlane(lds))
                : "memory", "m0");
 }

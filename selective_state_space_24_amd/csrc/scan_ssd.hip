@@ -163,11 +163,12 @@ struct StepArrays {
 // present, so it stays correct.
 // M0 (the LDS base of the load) is named as clobbered; clang warns that M0 is a reserved
 // register, which here only means that nothing else in the kernel may rely on its value across
-// the instruction (nothing does: the kernel has no other M0 user).
+// the instruction (nothing does: the kernel has no other M0 user). The compiler puts no wait states
+// into inline assembly: one stands between the write of M0 and the load that takes its base from it.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src),
                "s"(__builtin_amdgcn_readfirstlane(lds))
                : "memory", "m0");
 }

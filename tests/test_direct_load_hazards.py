@@ -89,6 +89,12 @@ def test_direct_loads_of_the_gated_delta_rule(found, kernel):
     assert not {k: n for k, n in hits.items() if n[1] or n[2]}
 
 
+def test_direct_loads_of_the_chunked_scan(found):
+    hits = {k: v for k, v in found.items() if "ssd_fwd_kernel" in k}
+    assert hits and all(n[0] > 0 for n in hits.values())
+    assert not {k: n for k, n in hits.items() if n[1] or n[2]}
+
+
 def test_the_check_itself():
     lines = ["0 <k>:", "\ts_mov_b32 m0, s4", "\tglobal_load_lds_dwordx4 v[0:1], off",
              "\ts_mov_b32 m0, s4", "\ts_nop 0", "\tglobal_load_lds_dwordx4 v[0:1], off",

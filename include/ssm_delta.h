@@ -35,6 +35,15 @@ extern "C" {
 
 #define SSM_DELTA_MAX_DSTATE 128
 
+/* Bits with which a value computed in fp32 (the state, a write, a weight within a chunk) enters a
+ * matrix product of a call on bf16 tensors. All sums are fp32 in either case, and no output depends
+ * on which other outputs are asked for. */
+enum ssm_delta_operands {
+  SSM_DELTA_OPERANDS_24 = 0, /* all of them: results as good as fp32 arithmetic makes them */
+  SSM_DELTA_OPERANDS_16 = 1  /* 2^-17 of a value lost in each product; the states too are good to
+                              * that. Faster (fp32 tensors: no difference). */
+};
+
 typedef struct ssm_delta_desc {
   int64_t batch;    /* >= 0 */
   int64_t seqlen;   /* L, >= 0 */
@@ -43,7 +52,8 @@ typedef struct ssm_delta_desc {
   int64_t dstate;   /* entries of a key, 1..SSM_DELTA_MAX_DSTATE */
   int64_t headdim;  /* entries of a value, >= 1 */
   int32_t io_dtype; /* ssm_dtype of q, k, v, g, beta and y */
-  int32_t reserved; /* 0 */
+  int32_t operands; /* ssm_delta_operands; not used by ssm_gated_delta_update, which has no
+                     * matrix products */
   int64_t q_stride_batch, q_stride_step, q_stride_group;
   int64_t k_stride_batch, k_stride_step, k_stride_group;
   int64_t v_stride_batch, v_stride_step, v_stride_head;

@@ -422,8 +422,9 @@ def selective_scan_bwd(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta
     return g
 
 
-from .delta import (SSM_DELTA_MAX_DSTATE, DeltaDesc, delta_desc_contiguous,  # noqa: E402,F401
-                    describe_delta, describe_delta_step, gated_delta_bwd, gated_delta_bwd_raw,
+from .delta import (SSM_DELTA_MAX_DSTATE, SSM_DELTA_OPERANDS_16,  # noqa: E402,F401
+                    SSM_DELTA_OPERANDS_24, DeltaDesc, delta_desc_contiguous, describe_delta,
+                    describe_delta_step, gated_delta_bwd, gated_delta_bwd_raw,
                     gated_delta_bwd_workspace_size, gated_delta_fwd, gated_delta_fwd_raw,
                     gated_delta_update, gated_delta_update_raw, gated_delta_workspace_size)
 from .norm import (NormDesc, layer_norm_bwd, layer_norm_bwd_raw,  # noqa: E402,F401

@@ -69,6 +69,7 @@ int64_t esize(const ssm_delta_desc& d) { return d.io_dtype == SSM_DTYPE_BF16 ? 2
 int check_desc(const ssm_delta_desc* d) {
   if (!d) return SSM_ERR_NULL_ARG;
   if (d->io_dtype != SSM_DTYPE_F32 && d->io_dtype != SSM_DTYPE_BF16) return SSM_ERR_BAD_DTYPE;
+  if (d->operands != SSM_DELTA_OPERANDS_24 && d->operands != SSM_DELTA_OPERANDS_16) return SSM_ERR_BAD_DTYPE;
   if (d->batch < 0 || d->seqlen < 0 || d->nheads < 1 || d->ngroups < 1 || d->nheads % d->ngroups ||
       d->dstate < 1 || d->dstate > SSM_DELTA_MAX_DSTATE || d->headdim < 1)
     return SSM_ERR_BAD_SHAPE;
@@ -145,6 +146,7 @@ void fill(const ssm_delta_desc& d, const void* q, const void* k, const void* v, 
   p->be_sb = d.beta_stride_batch; p->be_st = d.beta_stride_step; p->be_sh = d.beta_stride_head;
   p->nchunks = chunks(d);
   p->bf16 = d.io_dtype == SSM_DTYPE_BF16;
+  p->terms = d.operands == SSM_DELTA_OPERANDS_16 ? 2 : 3;
   p->nseg = 1;
   p->seg_chunks = p->nchunks;
   p->v_cols = value_pad(d);
@@ -267,7 +269,6 @@ int ssm_gated_delta_fwd(const ssm_delta_desc* desc, const void* q, const void* k
   // (row_access asks more of y than its 8-byte stores need)
   p.vec_y = row_access(d, d.headdim, y, shape_y(d).s);
   p.vec_state = d.dstate % 4 == 0 && aligned(s0, 16) && aligned(s_final, 16);
-  p.terms = s_final ? 3 : 2;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const FwdLayout lay = fwd_layout(d);
   p.rec = ws;

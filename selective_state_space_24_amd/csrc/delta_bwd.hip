@@ -160,7 +160,6 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
         P::load_terms_t(B + Lds::kRec + mat + tri_block(2 * kk, a0 >> 1) * block,
                         B + Lds::kRec + mat + tri_block(2 * kk + 1, a0 >> 1) * block, a0 + a, lane, t[a]);
     };
-    static_assert(Rec::kPTerms == NT, "");
     // dU
     f32x4 du[4];
 #pragma unroll

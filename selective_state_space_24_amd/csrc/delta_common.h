@@ -23,10 +23,9 @@
 //
 // Precision. MFMA accumulates in fp32. bf16 inputs are exact operands. Values computed in fp32
 // (S, R, U, T, P) enter a product as a sum of bf16 terms, each the bf16 of what the ones before
-// left: three terms carry all 24 bits, two carry 16. The products that S depends on use three
-// where a call returns a state in fp32, which is then as good as fp32 arithmetic makes it; where
-// all it returns is rounded to bf16 (8 bits), and in products that only y depends on, two. fp32 io
-// runs on the fp32 MFMA throughout.
+// left: three terms carry all 24 bits, so that every result is as good as fp32 arithmetic makes it
+// before its one rounding to the io type. A caller may choose two, which carry 16
+// (SSM_DELTA_OPERANDS_16). fp32 io runs on the fp32 MFMA throughout.
 #pragma once
 #include "delta_internal.h"
 #include "scan_kernels.h"
@@ -127,15 +126,13 @@ struct Eight {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// io bf16: exact operands are bf16, computed ones sums of bf16 terms, NT of them on the way to the
-// state
+// io bf16: exact operands are bf16, computed ones sums of NT bf16 terms
 template <int NT>
 struct Bf16 {
   typedef bf16_bits IO;
   static constexpr bool kBf16 = true;
   static constexpr int kFrag = 1024;    // bytes of a 16x32 fragment of an exact operand
   static constexpr int kTerms = NT;
-  static constexpr int kPTerms = 2;     // terms of P where only y depends on it
   typedef u32x4 Exact;
   template <int N>
   struct Terms {
@@ -375,7 +372,6 @@ struct F32 {
   static constexpr bool kBf16 = false;
   static constexpr int kFrag = 2048;
   static constexpr int kTerms = 1;
-  static constexpr int kPTerms = 1;
   typedef Eight Exact;
   template <int N>
   struct Terms {
@@ -536,15 +532,14 @@ struct F32 {
 };
 
 // A record: T's fragments (kTerms copies of each kFrag apart), P's, then per step e^G, e^{G_63 -
-// G}, beta and 1 for steps before L (else 0). The backward pass takes P with as many terms as T
-// (the gradient of the state depends on it) and G itself, as a sum of two floats.
+// G}, beta and 1 for steps before L (else 0). The backward pass takes G itself too, as a sum of two
+// floats.
 template <class P, bool BWD>
 struct Record {
-  static constexpr int kPTerms = BWD ? P::kTerms : P::kPTerms;
   static constexpr int kT = 0;
   static constexpr int kTBlock = P::kTerms * P::kFrag;
   static constexpr int kP = kTBlocks * kTBlock;
-  static constexpr int kPBlock = kPTerms * P::kFrag;
+  static constexpr int kPBlock = kTBlock;
   static constexpr int kRows = kP + kTBlocks * kPBlock;
   static constexpr int kGrow = 0, kDecay = kC * 4, kBeta = 2 * kC * 4, kOn = 3 * kC * 4;
   static constexpr int kGhi = 4 * kC * 4, kGlo = 5 * kC * 4;
@@ -598,6 +593,16 @@ __device__ __forceinline__ void store_state(float* col, int dk, bool vec, int g,
         if (r + i < dk) col[r + i] = S[a][i];
     }
   }
+}
+
+// Buffers of a scan's LDS: two of the operands where they have room beside two tiles of columns, or
+// beside one; else one of each.
+struct Buffers {
+  int n, tiles;
+};
+constexpr Buffers buffers(int bytes, int tile) {
+  constexpr int kLds = 160 * 1024;
+  return 2 * (bytes + tile) <= kLds ? Buffers{2, 2} : 2 * bytes + tile <= kLds ? Buffers{2, 1} : Buffers{1, 1};
 }
 
 // Brings the shared operands of a chunk into LDS by direct loads: NMAT matrices of 4 KK fragments

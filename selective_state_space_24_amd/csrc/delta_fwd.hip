@@ -136,16 +136,15 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaParams p) {
   }
   // where lane (g, c)'s four entries [t = 16w + c][16 j + 4g .. +4) go in fragment order
   const int a_t = row_tile(t), m_t = row_slot(t);
-  auto put = [&](int off, int bytes, bool of_t, int j, const f32x4 v) {
+  auto put = [&](int off, int bytes, int j, const f32x4 v) {
     uint8_t* f = rec + (off + tri_block(a_t, j >> 1) * bytes);
     const int gs = 2 * (j & 1) + (g >> 1);
-    if (of_t) P::template put4<P::kTerms>(f, gs, m_t, g & 1, v);
-    else P::template put4<Rec::kPTerms>(f, gs, m_t, g & 1, v);
+    P::template put4<P::kTerms>(f, gs, m_t, g & 1, v);
   };
   const int jmax = w | 1;  // a fragment covers two blocks of columns
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (j <= jmax) put(Rec::kP, Rec::kPBlock, false, j, pt[j]);
+    if (j <= jmax) put(Rec::kP, Rec::kPBlock, j, pt[j]);
   sync_lds();
 
   // T_ww: lane c solves for column c (the four lane groups alike)
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaParams p) {
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (j <= jmax) put(Rec::kT, Rec::kTBlock, true, j, tw[j]);
+    if (j <= jmax) put(Rec::kT, Rec::kTBlock, j, tw[j]);
 }
 
 // --- scan -----------------------------------------------------------------------------------------
@@ -201,7 +200,9 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaParams p) {
 // of them and needs nothing from the others but the shared left operands, which the workgroup
 // brings into LDS one chunk ahead (NBUF 2; where there is room for one buffer only, it waits for
 // its loads). Everything goes there by direct loads, v too, which is then read by columns; y leaves
-// four columns at a time one chunk late, so that nothing waits for it.
+// four columns at a time one chunk late, so that nothing waits for it. v is read at the start of a
+// chunk: where two buffers have room for one tile of v only, the next chunk's is loaded behind a
+// barrier in the middle of the chunk.
 //
 // Bound by the wavefronts' own matrix and vector instructions, which overlap little at the two
 // wavefronts a SIMD that the registers allow: batch 8, 4096 steps of 32 heads, 128 x 128 in bf16
@@ -237,9 +238,9 @@ struct ScanLds {
   // the part of the record that is not copied (P, without y) is left out
   static constexpr int kSkip = MODE == kY ? 0 : Rec::kRows - Rec::kP;
   static constexpr int kRows = kRec + Rec::kRows - kSkip;
-  static constexpr int kV = kRec + Rec::kBytes - kSkip;
-  static constexpr int kBytes = kV + Move::kTileBytes;
-  static constexpr int kBufs = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+  static constexpr int kBytes = kRec + Rec::kBytes - kSkip;
+  static constexpr Buffers kBuf = buffers(kBytes, Move::kTileBytes);
+  static constexpr int kAll = kBuf.n * kBytes + kBuf.tiles * Move::kTileBytes;
 };
 
 template <class P, int KK, int NW, Mode MODE>
@@ -251,9 +252,10 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
   constexpr bool STATES = MODE == kStates;
   constexpr bool SUMMARY = is_summary(MODE);
   constexpr bool Y = MODE == kY;
-  constexpr int NBUF = Lds::kBufs;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[NBUF * Lds::kBytes];
+  constexpr int NBUF = Lds::kBuf.n, VBUF = Lds::kBuf.tiles;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[Lds::kAll];
   lds_u8* const sm = (lds_u8*)smem;
+  auto tile_at = [&](int buf) { return sm + NBUF * Lds::kBytes + (VBUF == 2 ? buf : 0) * Lds::Move::kTileBytes; };
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // 32-bit arithmetic: there are fewer than 2^31 items
@@ -294,9 +296,12 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
   // chunk before. All at once they would queue up ahead of the wavefronts' first LDS reads.
   constexpr int kPoints = KK + 4;
   constexpr int kRec1 = Y ? Rec::kBytes / 1024 : Rec::kP / 1024, kRec2 = Y ? 0 : Rec::kRowBytes / 1024;
-  constexpr int kFragN = Lds::Move::kFragSteps, kTileN = Lds::Move::kTileSteps;
+  constexpr int kFragN = Lds::Move::kFragSteps, kTileN = VBUF == NBUF ? Lds::Move::kTileSteps : 0;
   constexpr int kRec1N = (kRec1 + NW - 1) / NW, kRec2N = (kRec2 + NW - 1) / NW;
   constexpr int kSteps = kFragN + kTileN + kRec1N + kRec2N;
+  auto load_tile = [&](int64_t ch, int i, lds_u8* to) {
+    if (!unit) mv.row_step(i, w, Vp + ch * kC * p.v_st + slice0, to);
+  };
   auto load_part = [&](int64_t ch, int buf, int first, int last) {
     lds_u8* const to = sm + buf * Lds::kBytes;
     const int64_t t0 = ch * kC;
@@ -305,12 +310,19 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
     for (int s = 0; s < kSteps; ++s) {
       if (s < first * kSteps / kPoints || s >= last * kSteps / kPoints) continue;
       if (s < kFragN) mv.frag_step(s, w, Kp + t0 * p.k_st, Qp + t0 * p.q_st, to + Lds::kK);
-      else if (s < kFragN + kTileN) {
-        if (!unit) mv.row_step(s - kFragN, w, Vp + t0 * p.v_st + slice0, to + Lds::kV);
-      } else if (s < kFragN + kTileN + kRec1N)
+      else if (s < kFragN + kTileN)
+        load_tile(ch, s - kFragN, tile_at(buf));
+      else if (s < kFragN + kTileN + kRec1N)
         Lds::Move::template run_step<kRec1>(s - kFragN - kTileN, w, lane, rc, to + Lds::kRec);
       else
         Lds::Move::template run_step<kRec2>(s - kFragN - kTileN - kRec1N, w, lane, rc + Rec::kRows, to + Lds::kRows);
+    }
+  };
+  // the tile of v, where it is not among the parts
+  auto load_late_tile = [&](int64_t ch) {
+    if constexpr (VBUF != NBUF) {
+#pragma unroll
+      for (int i = 0; i < Lds::Move::kTileSteps; ++i) load_tile(ch, i, tile_at(0));
     }
   };
   // before the parts of a last, shorter chunk
@@ -339,6 +351,7 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
   place(kC);
   load_first(c0);
   load_part(c0, 0, 0, kPoints);
+  load_late_tile(c0);
   wait_vmem_all();
   sync_lds();
 
@@ -348,7 +361,7 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
     f32x4 vf[4];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      vf[a] = P::template load_col4<Lds::Move::kPitch>(B + Lds::kV, tile_row4(a, g), 16 * w, c);
+      vf[a] = P::template load_col4<Lds::Move::kPitch>(tile_at(buf), tile_row4(a, g), 16 * w, c);
       if constexpr (!Y) {  // zeros in columns of the identity, and past the image's last
 #pragma unroll
         for (int i = 0; i < 4; ++i) vf[a][i] = live ? vf[a][i] : 0.0f;
@@ -377,7 +390,6 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
     // wavefronts to a SIMD the wait for a group read where it is used would show.
     typedef typename P::Exact Exact;
     typedef typename P::template Terms<NT> TermsT;
-    typedef typename P::template Terms<Rec::kPTerms> TermsP;
     auto get_rows = [&](Exact (&f)[4], int mat, int kk) {
 #pragma unroll
       for (int a = 0; a < 4; ++a) f[a] = P::load_frag(B + mat + (a * KK + kk) * P::kFrag, lane);
@@ -387,7 +399,7 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
       for (int a = 2 * kk; a < 4; ++a)
         P::load_terms(B + Lds::kRec + Rec::kT + tri_block(a, kk) * Rec::kTBlock, lane, t[a - 2 * kk]);
     };
-    auto get_p = [&](TermsP* t, int kk) {
+    auto get_p = [&](TermsT* t, int kk) {
 #pragma unroll
       for (int a = 2 * kk; a < 4; ++a)
         P::load_terms(B + Lds::kRec + Rec::kP + tri_block(a, kk) * Rec::kPBlock, lane, t[a - 2 * kk]);
@@ -424,7 +436,13 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
       point(kk);
       __builtin_amdgcn_sched_barrier(0);
       P::template mma_rows<NT>(fk[kk % kKeep], s, ks);
-      if constexpr (Y) P::template mma_rows<2>(fq[kk % kKeep], s, y);
+      if constexpr (Y) P::template mma_rows<NT>(fq[kk % kKeep], s, y);
+    }
+    if constexpr (VBUF != NBUF) {
+      if (more) {
+        sync_lds();  // every wavefront has read its columns of v
+        load_late_tile(ch + 1);
+      }
     }
     // R (beta is 0 for rows past the last step), and e^G (Q S) scale
 #pragma unroll
@@ -440,7 +458,7 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
     // U = T R
     f32x4 u[4];
     Exact kt[2][kRows];
-    TermsP p0[4], p1[2];
+    TermsT p0[4], p1[2];
 #pragma unroll
     for (int a = 0; a < 4; ++a) u[a] = f32x4{0, 0, 0, 0};
     {
@@ -491,7 +509,7 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
         P::template mma_rows<NT>(kt[n & 1], e, S + grp * kRows);
       }
       if constexpr (Y) {
-        typename P::template Terms<2> uu;
+        TermsT uu;
         if (kk == 0) get_p(p1, 1);
         P::split(u[2 * kk], u[2 * kk + 1], uu);
         __builtin_amdgcn_sched_barrier(0);

@@ -51,7 +51,7 @@ struct DeltaParams {
   int32_t vec_y;     // rows of y (dv) allow 8-byte access and dv is a multiple of 4
   int32_t vec_state; // states allow 16-byte access and dk is a multiple of 4
   int32_t bf16;
-  int32_t terms;     // bf16 terms of what the state depends on: 3 where a state is returned, else 2
+  int32_t terms;     // bf16 terms of a computed operand: 3, or 2 where the caller chose 16 bits
 };
 
 // The backward pass: the forward's arguments (y's strides are dy's) and the gradients, written

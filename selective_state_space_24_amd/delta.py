@@ -12,13 +12,14 @@ from typing import Optional
 from . import _abi
 
 SSM_DELTA_MAX_DSTATE = 128
+SSM_DELTA_OPERANDS_24, SSM_DELTA_OPERANDS_16 = 0, 1
 
 
 class DeltaDesc(ctypes.Structure):
     """Mirror of ``ssm_delta_desc``."""
     _fields_ = ([(n, ctypes.c_int64) for n in
                  ("batch", "seqlen", "nheads", "ngroups", "dstate", "headdim")]
-                + [("io_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                + [("io_dtype", ctypes.c_int32), ("operands", ctypes.c_int32)]
                 + [(f"{t}_stride_{d}", ctypes.c_int64) for t, inner in
                    (("q", "group"), ("k", "group"), ("v", "head"), ("g", "head"),
                     ("beta", "head"), ("y", "head")) for d in ("batch", "step", inner)])
@@ -169,19 +170,31 @@ def _check_state(name, t, desc, device):
     _abi.check_f32(name, t, (desc.batch, desc.nheads, desc.headdim, desc.dstate), device)
 
 
+def _operands(bits: int) -> int:
+    if bits == 24:
+        return SSM_DELTA_OPERANDS_24
+    if bits == 16:
+        return SSM_DELTA_OPERANDS_16
+    raise ValueError(f"operand_bits must be 24 or 16, got {bits}")
+
+
 def gated_delta_fwd(q, k, v, g, beta, scale: Optional[float] = None, *, s0=None, final_state=None,
-                    out=None, workspace=None, stream=None):
+                    out=None, operand_bits: int = 24, workspace=None, stream=None):
     """y of the gated delta rule, with S_t = exp(g_t) S_(t-1) + u_t k_t^T, u_t = beta_t (v_t -
     exp(g_t) S_(t-1) k_t) and y_t = scale S_t q_t.
 
     ``scale`` defaults to dstate ** -0.5. ``s0`` is the initial state. ``final_state`` is True
     (allocate) or a tensor that receives the state after the last step; the call then returns
-    ``(y, final_state)``. ``out`` receives y if given. ``workspace`` may be a uint8 device tensor
+    ``(y, final_state)``; y is the same either way. ``out`` receives y if given. ``operand_bits`` is
+    how many bits of a value computed in fp32 enter the matrix products of a call on bfloat16 tensors:
+    all 24, or 16, which is faster and leaves y before its rounding, and the states, good to about
+    2^-17. ``workspace`` may be a uint8 device tensor
     of at least ``gated_delta_workspace_size`` bytes; otherwise one is allocated. ``stream``
     defaults to the current torch stream. Raises ScanError with the library's status on failure.
     """
     torch = _abi.torch()
     desc = describe_delta(q, k, v, g, beta, out)
+    desc.operands = _operands(operand_bits)
     if s0 is not None:
         _check_state("s0", s0, desc, v.device)
     if final_state is not None and not isinstance(final_state, bool):

@@ -240,3 +240,13 @@ def test_reference_gradients_against_differences(name):
 
     e = 1e-5  # error of a central difference: e^2 f''' / 6 + 1e-16 f / e, both about 1e-10
     assert abs((loss(e) - loss(-e)) / (2 * e) - got) <= 1e-7 * max(1.0, abs(got))
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd], ids=["fwd", "bwd"])
+def test_delta_refuses_operands_that_do_not_exist(call):
+    assert call(_desc(operands=2)) == -3
+    assert call(_desc(operands=-1)) == -3
+    assert call(_desc(operands=ssm.SSM_DELTA_OPERANDS_16), ws=None) == -7
+    with pytest.raises(ValueError, match="operand_bits"):
+        ins = make(2, 10, 4, 2, 16, 8, torch.float32)
+        ssm.gated_delta_fwd(*[ins[n] for n in ("q", "k", "v", "g", "beta")], operand_bits=32)

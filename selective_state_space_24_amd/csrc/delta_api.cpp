@@ -193,7 +193,7 @@ BwdLayout bwd_layout(const ssm_delta_desc& d) {
   fill(d, nullptr, nullptr, nullptr, nullptr, nullptr, 0.0f, &p);
   ssm::delta_plan(&p);
   const size_t items = (size_t)d.batch * d.nheads * p.nchunks;
-  const size_t img = items * ssm::delta_image_bytes(p.bf16, d.dstate, d.headdim);
+  const size_t img = items * ssm::delta_image_bytes(d.dstate, d.headdim);
   BwdLayout l;
   l.nseg = p.nseg;
   l.seg_chunks = p.seg_chunks;
@@ -358,7 +358,6 @@ int ssm_gated_delta_bwd(const ssm_delta_desc* desc, const void* q, const void* k
   p.vec_dv = d.headdim % 4 == 0 && aligned(dv, 8);
   p.vec_out = d.dstate % 8 == 0 && aligned(dq, 16) && aligned(dk, 16);
   p.f.vec_state = d.dstate % 4 == 0 && aligned(s0, 16) && aligned(ds_final, 16) && aligned(ds0, 16);
-  p.f.terms = ds0 ? 3 : 2;
   ssm::DeltaPack list;
   uint8_t* room = ws + lay.copies;
   pack_inputs(d, &p.f, room, &list);

@@ -32,14 +32,14 @@ struct BackLds {
   static constexpr int kQ = 4 * KK * P::kFrag;
   static constexpr int kRec = 2 * kQ;
   static constexpr int kRows = kRec + Rec::kRows;
-  static constexpr int kDY = kRec + Rec::kBytes;
-  static constexpr int kBytes = kDY + Move::kTileBytes;
-  static constexpr int kBufs = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+  static constexpr int kBytes = kRec + Rec::kBytes;
+  static constexpr Buffers kBuf = buffers(kBytes, Move::kTileBytes);  // tiles of dY
+  static constexpr int kAll = kBuf.n * kBytes + kBuf.tiles * Move::kTileBytes;
 };
 
-// Bound as the forward scan is; four products to its five, with T and P transposed on the way out of
-// LDS: 680 us for batch 4, 8192 steps of 64 heads, 128 x 64 in bf16, of which 1.6 GB of image
-// written take 330 us at a copy's rate.
+// Four products to the forward scan's five, with T and P transposed on the way out of LDS: 760 us for
+// batch 4, 8192 steps of 64 heads, 128 x 64 in bf16 (680 with 16-bit operands), of which 1.6 GB of
+// image written take 330 us at a copy's rate.
 //
 // dV leaves a chunk late, as the forward scan's y does. Where the sequence is split, a first run
 // (LOCAL) makes what each segment but the first adds to the gradient of the state before it, from
@@ -50,10 +50,11 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
   typedef BackLds<P, KK, NW> Lds;
   typedef typename Lds::Rec Rec;
   constexpr int NT = P::kTerms;
-  constexpr int NBUF = Lds::kBufs;
+  constexpr int NBUF = Lds::kBuf.n, YBUF = Lds::kBuf.tiles;
   const DeltaParams& p = q.f;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[NBUF * Lds::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[Lds::kAll];
   lds_u8* const sm = (lds_u8*)smem;
+  auto tile_at = [&](int buf) { return sm + NBUF * Lds::kBytes + (YBUF == 2 ? buf : 0) * Lds::Move::kTileBytes; };
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // 32-bit arithmetic: there are fewer than 2^31 items
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
   };
   // the loads of a chunk in parts, as in the forward scan
   constexpr int kPoints = KK + 4;
-  constexpr int kFragN = Lds::Move::kFragSteps, kTileN = Lds::Move::kTileSteps;
+  constexpr int kFragN = Lds::Move::kFragSteps, kTileN = YBUF == NBUF ? Lds::Move::kTileSteps : 0;
   constexpr int kSteps = kFragN + kTileN + (Rec::kBytes / 1024 + NW - 1) / NW;
   auto load_part = [&](int64_t ch, int buf, int first, int last) {
     lds_u8* const to = sm + buf * Lds::kBytes;
@@ -97,10 +98,16 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
     for (int s = 0; s < kSteps; ++s) {
       if (s < first * kSteps / kPoints || s >= last * kSteps / kPoints) continue;
       if (s < kFragN) mv.frag_step(s, w, Kp + t0 * p.k_st, Qp + t0 * p.q_st, to + Lds::kK);
-      else if (s < kFragN + kTileN) mv.row_step(s - kFragN, w, DYp + t0 * p.y_st + slice0, to + Lds::kDY);
+      else if (s < kFragN + kTileN) mv.row_step(s - kFragN, w, DYp + t0 * p.y_st + slice0, tile_at(buf));
       else
         Lds::Move::template run_step<Rec::kBytes / 1024>(s - kFragN - kTileN, w, lane,
                                                          rec + ch * (int64_t)Rec::kBytes, to + Lds::kRec);
+    }
+  };
+  auto load_late_tile = [&](int64_t ch) {
+    if constexpr (YBUF != NBUF) {
+#pragma unroll
+      for (int i = 0; i < Lds::Move::kTileSteps; ++i) mv.row_step(i, w, DYp + ch * kC * p.y_st + slice0, tile_at(0));
     }
   };
 
@@ -117,6 +124,7 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
   };
   place((int)(L - (c1 - 1) * kC < kC ? L - (c1 - 1) * kC : kC));
   load_part(c1 - 1, 0, 0, kPoints);
+  load_late_tile(c1 - 1);
   place(kC);
   wait_vmem_all();
   sync_lds();
@@ -129,7 +137,7 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const f32x4 on = lds16f(rows + Rec::kOn + tile_row4(a, g) * 4);
-      d[a] = P::template load_col4<Lds::Move::kPitch>(B + Lds::kDY, tile_row4(a, g), 16 * w, c);
+      d[a] = P::template load_col4<Lds::Move::kPitch>(tile_at(buf), tile_row4(a, g), 16 * w, c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[a][i] = live && on[i] != 0.0f ? d[a][i] : 0.0f;
     }
@@ -142,7 +150,7 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
     if (image) {
       uint8_t* im = image + ch * img_chunk + Image<P, KK>::kS + img_s;
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) P::template put_image<2>(im + kk * Image<P, KK>::kFrag, lane, S[2 * kk], S[2 * kk + 1]);
+      for (int kk = 0; kk < KK; ++kk) P::put_kept(im + kk * Image<P, KK>::kFrag, lane, S[2 * kk], S[2 * kk + 1]);
     }
     if constexpr (!LOCAL) {
       if (ch + 1 < c1) store_late(ch + 1);
@@ -176,6 +184,12 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
       point(kk);
       __builtin_amdgcn_sched_barrier(0);
       P::template mma_rows<NT>(fk[kk & 1], s, du);
+    }
+    if constexpr (YBUF != NBUF) {
+      if (more) {
+        sync_lds();  // every wavefront has read its columns of dY
+        load_late_tile(ch - 1);
+      }
     }
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
@@ -218,7 +232,7 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
     if (image) {
       uint8_t* im = image + ch * img_chunk + Image<P, KK>::kU + img_u;
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) P::template put_image<2>(im + kk * Image<P, KK>::kFrag, lane, dr[2 * kk], dr[2 * kk + 1]);
+      for (int kk = 0; kk < 2; ++kk) P::put_kept(im + kk * Image<P, KK>::kFrag, lane, dr[2 * kk], dr[2 * kk + 1]);
     }
     // dV, and the weighted rows of dY and dR
 #pragma unroll
@@ -295,11 +309,15 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
 // steps [16w, 16w + 16) as columns: with x a row of a tile and y = 16w + c its column, the first
 // makes the tiles E both ways round (x = s, y = t and x = t, y = s) and the second N; they hand
 // each other the weighted tiles through LDS, and each makes half the rows of its columns of dQ^T
-// and dK^T from them. The sums over v go in slices of 32 columns, brought into LDS one ahead.
+// and dK^T from them. The sums over v go in slices of 32 columns, brought into LDS one ahead. Images
+// kept in fp32 (bf16 io, three terms) come in staged: S and dS into a strip of LDS, U and dR into
+// registers, and each wavefront makes terms of its share once when the slice before has been read.
+// That is 24 values a lane; terms made by every wavefront of what it reads would be a hundred, and
+// terms kept in memory half as many bytes again to move.
 //
-// Bound by latency within the CU: K, Q and two slices take 145 KB of LDS, so one workgroup runs on
-// each. Batch 4, 8192 steps of 64 heads (16 of keys), 128 x 64 in bf16: 1.39 ms, 5 % less if the
-// same slice is read every time.
+// Bound by latency within the CU: the LDS (153 KB with keys of 128, three terms; 145 KB with two)
+// leaves room for one workgroup on each. Batch 4, 8192 steps of 64 heads (16 of keys), 128 x 64 in
+// bf16: 1.94 ms, with 16-bit operands 1.4 ms (5 % less if the same slice is read every time).
 template <class P, int KK>
 struct GradLds {
   typedef Image<P, KK> Img;
@@ -307,16 +325,21 @@ struct GradLds {
   static constexpr int kQ = 4 * KK * P::kFrag;
   static constexpr int kSlice = 2 * kQ;
   // a slice: the image (S, U), the second one (dS, dR), dY
-  static constexpr int kImgB = Img::kBytes;
-  static constexpr int kDY = 2 * Img::kBytes;
-  static constexpr int kSliceBytes = kDY + 4 * P::kFrag;
-  static constexpr int kTerms = P::template kImageFrag<2>;  // a right operand handed over
+  static constexpr int kFrag = P::template kImageFrag<P::kTerms>;
+  static constexpr int kS = 0, kU = 2 * KK * kFrag, kImg = kU + 4 * kFrag;
+  static constexpr int kDYBytes = 4 * P::kFrag;
+  static constexpr int kSliceBytes = 2 * kImg + (P::kStaged ? 0 : kDYBytes);
+  static constexpr int kTerms = kFrag;      // a right operand handed over
   // the tiles are handed over in the buffer of the slice before
   static constexpr int kHandBytes = 4 * 6 * kTerms;
   static constexpr int kBuffer = kSliceBytes > kHandBytes ? kSliceBytes : kHandBytes;
+  // staged: the next slice's S and dS in fp32, its U and dR in registers, and two slots for dY
+  static constexpr int kStage = P::kStaged ? 2 * 2 * KK * Img::kFrag : 0;
   static constexpr int kRest = 2 * 8 * kC * 4 + (6 * kC + 8) * 4;  // rows of two heads, sums
-  static constexpr int kBufs = kSlice + 2 * kBuffer + kRest <= 160 * 1024 ? 2 : 1;
-  static constexpr int kRows = kSlice + kBufs * kBuffer;
+  static constexpr int kBufs = !P::kStaged && kSlice + 2 * kBuffer + kRest <= 160 * 1024 ? 2 : 1;
+  static constexpr int kStageAt = kSlice + kBufs * kBuffer;
+  static constexpr int kDYAt = kStageAt + kStage;
+  static constexpr int kRows = kDYAt + (P::kStaged ? 2 * kDYBytes : 0);
   static constexpr int kSums = kRows + 2 * 8 * kC * 4;
   static constexpr int kBytes = kRows + kRest;
 };
@@ -331,7 +354,8 @@ template <class P, int KK>
 __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q) {
   typedef typename P::IO IO;
   typedef typename P::Exact Exact;
-  typedef typename P::template Terms<2> Terms2;
+  constexpr int NT = P::kTerms;
+  typedef typename P::template Terms<NT> TermsT;
   typedef GradLds<P, KK> Lds;
   typedef Record<P, true> Rec;
   typedef Image<P, KK> Img;
@@ -367,20 +391,36 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
       P::store_frag(sm + f * P::kFrag, lane, P::load8(row + 32 * kk + 8 * g));
     }
   }
-  // slice sl of the r-th head of the group; with the first of a head, the rows of its record
+  // Slice sl of the r-th head of the group, with the first of a head the rows of its record: into
+  // buffer `buf`; or, staged, to where the wavefront that will make terms of it finds its part, and dY
+  // into slot `buf`.
+  f32x4 raw_a, raw_b;  // a fragment of U (first wavefronts) or dR
   auto load_slice = [&](int r, int sl, int buf) {
     lds_u8* const to = sm + Lds::kSlice + buf * Lds::kBuffer;
+    lds_u8* const dy_at = P::kStaged ? sm + Lds::kDYAt + buf * Lds::kDYBytes : to + 2 * Lds::kImg;
     const int64_t h = (int64_t)grp * rep + r, bhc = (b * p.nheads + h) * nch + ch;
     const int64_t at = (bhc * slices + sl) * Img::kBytes;
-    Move::template run<Img::kBytes / 1024>(wave, lane, p.image + at, to);
-    Move::template run<Img::kBytes / 1024>(wave, lane, q.image_b + at, to + Lds::kImgB);
+    if constexpr (P::kStaged) {
+      if (wave < 2 * KK) {
+        const int f = wave * Img::kFrag;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t unit = (uint32_t)(uintptr_t)(sm + Lds::kStageAt + 2 * f + half * 1024);
+          dma16(p.image + at + Img::kS + f, half * 1024 + lane * 16, unit);
+          dma16(q.image_b + at + Img::kS + f, half * 1024 + lane * 16, unit + Img::kFrag);
+        }
+      }
+    } else {
+      Move::template run<Img::kBytes / 1024>(wave, lane, p.image + at, to);
+      Move::template run<Img::kBytes / 1024>(wave, lane, q.image_b + at, to + Lds::kImg);
+    }
     if (sl == 0)
       Move::template run<2>(wave, lane, p.rec + bhc * (int64_t)Rec::kBytes + Rec::kRows,
                             sm + Lds::kRows + (r & 1) * 2048);
     if (wave < 4) {
       const int x = tile_row(w, c);
       const IO* row = static_cast<const IO*>(q.dy) + b * p.y_sb + h * p.y_sh + (t0 + (x < n ? x : n - 1)) * p.y_st;
-      lds_u8* const f = to + Lds::kDY + w * P::kFrag;
+      lds_u8* const f = dy_at + w * P::kFrag;
       if (direct_y) {
 #pragma unroll
         for (int half = 0; half < P::kFrag / 1024; ++half)
@@ -389,6 +429,29 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
         P::store_frag(f, lane, sl * 32 + 8 * g < cols ? P::load8(row + sl * 32 + 8 * g) : Exact{});
       }
     }
+    if constexpr (P::kStaged) {
+      const uint8_t* f = (part ? q.image_b : p.image) + at + Img::kU + w * Img::kFrag + lane * 16;
+      raw_a = *reinterpret_cast<const f32x4*>(f);
+      raw_b = *reinterpret_cast<const f32x4*>(f + 1024);
+    }
+  };
+  // staged: the wavefront's fragments as terms into the buffer; returns its share of <S, dS>
+  auto make_terms = [&]() {
+    float dot = 0.0f;
+    if constexpr (P::kStaged) {
+      lds_u8* const to = sm + Lds::kSlice;
+      if (wave < 2 * KK) {
+        const lds_u8* const from = sm + Lds::kStageAt + 2 * wave * Img::kFrag + lane * 16;
+        const f32x4 sa = lds16f(from), sb = lds16f(from + 1024);
+        const f32x4 da = lds16f(from + Img::kFrag), db = lds16f(from + Img::kFrag + 1024);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dot = fmaf(sa[i], da[i], fmaf(sb[i], db[i], dot));
+        P::template put_image<NT>(to + Lds::kS + wave * Lds::kFrag, lane, sa, sb);
+        P::template put_image<NT>(to + Lds::kImg + Lds::kS + wave * Lds::kFrag, lane, da, db);
+      }
+      P::template put_image<NT>(to + part * Lds::kImg + Lds::kU + w * Lds::kFrag, lane, raw_a, raw_b);
+    }
+    return dot;
   };
   // lane (g, c)'s fragment of row y = 16w + c
   const int a_y = row_tile(16 * w + c), l_y = g * 16 + row_slot(16 * w + c);
@@ -418,33 +481,38 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
     for (int sl = 0; sl < slices; ++sl) {
       wait_vmem_all();
       sync_lds();
-      const lds_u8* const B = sm + Lds::kSlice + buf * Lds::kBuffer;
+      if constexpr (P::kStaged) {
+        ss += make_terms();
+        sync_lds();
+      }
+      const lds_u8* const B = sm + Lds::kSlice + (NBUF == 2 ? buf : 0) * Lds::kBuffer;
+      const lds_u8* const iY = P::kStaged ? sm + Lds::kDYAt + buf * Lds::kDYBytes : B + 2 * Lds::kImg;
       Exact vv = {};
       if (part == 0 && sl * 32 + 8 * g < cols) vv = P::load8(vrow + sl * 32 + 8 * g);
-      if constexpr (NBUF == 2) {
+      if constexpr (NBUF == 2 || P::kStaged) {
         if (sl + 1 < slices) load_slice(r, sl + 1, buf ^ 1);
         else if (r + 1 < rep) load_slice(r + 1, 0, buf ^ 1);
       }
 
-      const lds_u8 *const iS = B + Img::kS, *const iU = B + Img::kU;
-      const lds_u8 *const iD = B + Lds::kImgB + Img::kS, *const iR = B + Lds::kImgB + Img::kU;
-      const Exact yb = P::load_frag(B + Lds::kDY + a_y * P::kFrag, l_y);
-      Terms2 ub, rb;
+      const lds_u8 *const iS = B + Lds::kS, *const iU = B + Lds::kU;
+      const lds_u8 *const iD = B + Lds::kImg + Lds::kS, *const iR = B + Lds::kImg + Lds::kU;
+      const Exact yb = P::load_frag(iY + a_y * P::kFrag, l_y);
+      TermsT ub, rb;
       P::load_image_block(iU, 2, w, lane, ub);
       P::load_image_block(iR, 2, w, lane, rb);
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
         if ((a >> 1) <= (w >> 1)) {
-          Terms2 ua;
+          TermsT ua;
           P::load_image_tile(iU, 2, a, lane, ua);
           if (part == 0) m1[a] = P::mma_te(ua, yb, m1[a]);
           else m1[a] = P::mma_tt(ua, rb, m1[a]);
         }
         if ((a >> 1) >= (w >> 1)) {
           if (part == 0) {
-            m2[a] = P::template mma<2>(P::load_frag(B + Lds::kDY + a * P::kFrag, lane), ub, m2[a]);
+            m2[a] = P::template mma<NT>(P::load_frag(iY + a * P::kFrag, lane), ub, m2[a]);
           } else {
-            Terms2 ra;
+            TermsT ra;
             P::load_image_tile(iR, 2, a, lane, ra);
             m2[a] = P::mma_tt(ra, ub, m2[a]);
           }
@@ -453,7 +521,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
       if (has) {
 #pragma unroll
         for (int a = 0; a < kTiles; ++a) {
-          Terms2 s, d;
+          TermsT s, d;
           P::load_image_tile(iS, KK, a0 + a, lane, s);
           P::load_image_tile(iD, KK, a0 + a, lane, d);
           sy[a] = P::mma_te(s, yb, sy[a]);
@@ -468,13 +536,15 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
 #pragma unroll
         for (int e = 0; e < 8; ++e) rv = fmaf(x[e], z[e], rv);
       }
-      for (int f = wave; f < 2 * KK; f += 8) {
-        P::image_floats(iS + f * Img::kFrag, lane, x);
-        P::image_floats(iD + f * Img::kFrag, lane, z);
+      if constexpr (!P::kStaged) {
+        for (int f = wave; f < 2 * KK; f += 8) {
+          P::image_floats(iS + f * Lds::kFrag, lane, x);
+          P::image_floats(iD + f * Lds::kFrag, lane, z);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], z[e], ss);
+          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], z[e], ss);
+        }
       }
-      if constexpr (NBUF == 1) {
+      if constexpr (NBUF == 1 && !P::kStaged) {
         if (sl + 1 < slices) {
           sync_lds();
           load_slice(r, sl + 1, 0);
@@ -541,7 +611,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
     }
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      Terms2 x;
+      TermsT x;
       P::split(m1[2 * kk], m1[2 * kk + 1], x);
       P::store_terms(hand + ((part ? 4 : 0) + kk) * Lds::kTerms, lane, x);
       if (part == 0) {
@@ -586,7 +656,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
     if (has) {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        Terms2 x1, x2, x3;
+        TermsT x1, x2, x3;
         P::load_terms(hand + kk * Lds::kTerms, lane, x1);
         P::load_terms(hand + (2 + kk) * Lds::kTerms, lane, x2);
         P::load_terms(hand + (4 + kk) * Lds::kTerms, lane, x3);
@@ -600,9 +670,9 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
             kt[i] = P::load_frag_t(sm + Lds::kK + f0, sm + Lds::kK + f1, a, lane);
             qt[i] = P::load_frag_t(sm + Lds::kQ + f0, sm + Lds::kQ + f1, a, lane);
           }
-          P::template mma_rows<2>(kt, x1, dq + j);
-          P::template mma_rows<2>(kt, x3, dkk + j);
-          P::template mma_rows<2>(qt, x2, dkk + j);
+          P::template mma_rows<NT>(kt, x1, dq + j);
+          P::template mma_rows<NT>(kt, x3, dkk + j);
+          P::template mma_rows<NT>(qt, x2, dkk + j);
         }
       }
     }
@@ -627,7 +697,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
         store_elem(static_cast<IO*>(q.dbeta) + out + lane * p.nheads, *sums(2 * kC + lane) + *sums(3 * kC + lane));
       }
     }
-    if constexpr (NBUF == 1) {
+    if constexpr (NBUF == 1 && !P::kStaged) {
       if (r + 1 < rep) {
         sync_lds();  // the handed tiles have been read
         load_slice(r + 1, 0, 0);

@@ -227,6 +227,17 @@ struct Bf16 {
   // bytes of an image fragment of N terms
   template <int N>
   static constexpr int kImageFrag = N * 1024;
+  // What the backward pass keeps in memory: two terms, or, for three, fp32, which is less to move; the
+  // gradient kernel makes terms of it on the way in.
+  static constexpr bool kStaged = NT == 3;
+  static __device__ __forceinline__ void put_kept(uint8_t* f, int lane, const f32x4 a, const f32x4 b) {
+    if constexpr (kStaged) {
+      *reinterpret_cast<f32x4*>(f + lane * 16) = a;
+      *reinterpret_cast<f32x4*>(f + 1024 + lane * 16) = b;
+    } else {
+      put_image<2>(f, lane, a, b);
+    }
+  }
   // Where lane (g, c)'s 16 bytes of an image fragment lie: slots of odd groups in another order and
   // the 8-byte halves of the last two groups exchanged, so that a transposed read, which takes one
   // half of 8 slots of each group, meets every bank alike.
@@ -281,6 +292,14 @@ struct Bf16 {
     for (int n = 0; n < N; ++n)
       *reinterpret_cast<u32x4*>(f + n * 1024 + image_slot(lane >> 4, lane & 15) * 16) = image_halves(lane >> 4, t.t[n]);
   }
+  // the same in LDS
+  template <int N>
+  static __device__ __forceinline__ void put_image(lds_u8* f, int lane, const f32x4 a, const f32x4 b) {
+    Terms<N> t;
+    split(a, b, t);
+#pragma unroll
+    for (int n = 0; n < N; ++n) sts16(f + n * 1024 + image_slot(lane >> 4, lane & 15) * 16, image_halves(lane >> 4, t.t[n]));
+  }
   static __device__ __forceinline__ void floats(const u32x4 w, float (&f)[8]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -288,12 +307,16 @@ struct Bf16 {
       f[2 * e + 1] = hi_f(w[e]);
     }
   }
-  static __device__ __forceinline__ void floats(const Terms<2>& t, float (&f)[8]) {
-    float l[8];
+  template <int N>
+  static __device__ __forceinline__ void floats(const Terms<N>& t, float (&f)[8]) {
     floats(t.t[0], f);
-    floats(t.t[1], l);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] += l[e];
+    for (int n = 1; n < N; ++n) {
+      float l[8];
+      floats(t.t[n], l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] += l[e];
+    }
   }
   static __device__ __forceinline__ Exact exact(const f32x4 a, const f32x4 b) {
     return u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(b[0], b[1]),
@@ -342,7 +365,7 @@ struct Bf16 {
   }
   // eight floats of an image fragment in LDS (some eight; each lane other ones)
   static __device__ __forceinline__ void image_floats(const lds_u8* f, int lane, float (&v)[8]) {
-    Terms<2> t;
+    Terms<NT> t;
     load_terms(f, lane, t);
     floats(t, v);
   }
@@ -453,6 +476,10 @@ struct F32 {
   }
   template <int N>
   static constexpr int kImageFrag = 2048;
+  static constexpr bool kStaged = false;
+  static __device__ __forceinline__ void put_kept(uint8_t* f, int lane, const f32x4 a, const f32x4 b) {
+    put_image<1>(f, lane, a, b);
+  }
   template <int N>
   static __device__ __forceinline__ void load_image_tile(const lds_u8* part, int nk, int a, int lane,
                                                          Terms<N>& r) {
@@ -494,7 +521,8 @@ struct F32 {
       f[4 + e] = w.b[e];
     }
   }
-  static __device__ __forceinline__ void floats(const Terms<2>& t, float (&f)[8]) { floats(t.t, f); }
+  template <int N>
+  static __device__ __forceinline__ void floats(const Terms<N>& t, float (&f)[8]) { floats(t.t, f); }
   static __device__ __forceinline__ Exact exact(const f32x4 a, const f32x4 b) { return Eight{a, b}; }
   static __device__ __forceinline__ void store8(IO* p, const f32x4 a, const f32x4 b) {
     *reinterpret_cast<f32x4*>(p) = a;
@@ -552,12 +580,12 @@ struct Record {
 // What the backward pass keeps of a chunk and 32 columns of v: the state before the chunk and U
 // (dS after it and dR, in the second of two such images), in fragments whose rows are the columns
 // of v: the fragment (tile, kk) holds at lane (g, c) the entries [32 kk + 8g .. +8) of column 16
-// tile + c, as a scan wavefront has them. With bf16 io they are kept in two terms: one (8 bits)
-// would do for dq and dk, but dg is a sum of such products of either sign (one step of one state of
-// one entry: 6.9e-3 off).
+// tile + c, as a scan wavefront has them, in 2 KB: fp32, or two bf16 terms where the caller chose 16
+// bits. One term (8 bits) would not do even there: dg is a sum of such products of either sign (one
+// step of one state of one entry: 6.9e-3 off).
 template <class P, int KK>
 struct Image {
-  static constexpr int kFrag = P::template kImageFrag<2>;
+  static constexpr int kFrag = 2048;
   static constexpr int kS = 0;
   static constexpr int kU = 2 * KK * kFrag;
   static constexpr int kBytes = kU + 4 * kFrag;

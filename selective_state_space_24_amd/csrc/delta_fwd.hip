@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
         uint8_t* im = image + ch * img_chunk;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
-          P::template put_image<2>(im + Image<P, KK>::kS + img_s + kk * Image<P, KK>::kFrag, lane, S[2 * kk], S[2 * kk + 1]);
+          P::put_kept(im + Image<P, KK>::kS + img_s + kk * Image<P, KK>::kFrag, lane, S[2 * kk], S[2 * kk + 1]);
       }
     } else if constexpr (Y) {
       if (ch > c0) store_late(ch - 1);
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(64 * NW) delta_scan_kernel(const DeltaParams p
       if (image) {
         uint8_t* im = image + ch * img_chunk + Image<P, KK>::kU + img_u;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) P::template put_image<2>(im + kk * Image<P, KK>::kFrag, lane, u[2 * kk], u[2 * kk + 1]);
+        for (int kk = 0; kk < 2; ++kk) P::put_kept(im + kk * Image<P, KK>::kFrag, lane, u[2 * kk], u[2 * kk + 1]);
       }
     }
     // S = e^{G_63} S + K^T (e^{G_63 - G} U), and Y += P U
@@ -732,9 +732,12 @@ size_t delta_record_bytes(bool bf16, bool bwd) {
   return bf16 ? Record<Bf16<3>, false>::kBytes : Record<F32, false>::kBytes;
 }
 
-size_t delta_image_bytes(bool bf16, int64_t dk, int64_t dv) {
-  const size_t frag = bf16 ? Bf16<2>::kImageFrag<2> : F32::kImageFrag<2>;
-  return (size_t)((dv + 31) / 32) * (2 * delta_pad_key(dk) / 32 + 4) * frag;
+size_t delta_image_bytes(int64_t dk, int64_t dv) {
+  switch (delta_pad_key(dk)) {
+    case 32: return (size_t)((dv + 31) / 32) * Image<F32, 1>::kBytes;
+    case 64: return (size_t)((dv + 31) / 32) * Image<F32, 2>::kBytes;
+    default: return (size_t)((dv + 31) / 32) * Image<F32, 4>::kBytes;
+  }
 }
 
 // Columns per workgroup: as many as leave a workgroup for every CU (a wider one reads K, Q, T and

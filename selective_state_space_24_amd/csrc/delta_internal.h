@@ -82,7 +82,7 @@ DeltaSplitLayout delta_split_layout(const DeltaParams& p);
 // Bytes of one record of the forward or the backward pass, and of an image per (batch, head,
 // chunk).
 size_t delta_record_bytes(bool bf16, bool bwd);
-size_t delta_image_bytes(bool bf16, int64_t dk, int64_t dv);
+size_t delta_image_bytes(int64_t dk, int64_t dv);
 // Wavefronts (16 columns of v each) per workgroup of the scans: 4 or 8.
 int delta_scan_waves(const DeltaParams& p);
 

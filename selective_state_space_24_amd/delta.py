@@ -232,12 +232,14 @@ def gated_delta_update(state, q, k, v, g, beta, scale: Optional[float] = None, *
 
 
 def gated_delta_bwd(q, k, v, g, beta, dy, scale: Optional[float] = None, *, s0=None, ds_final=None,
-                    want_ds0: bool = False, workspace=None, stream=None) -> dict:
+                    want_ds0: bool = False, operand_bits: int = 24, workspace=None, stream=None) -> dict:
     """Gradients of ``gated_delta_fwd`` for dy, the gradient of y, and ``ds_final``, that of its
     final state if given. A dy that was expanded (stride 0) is copied first. Returns a dict of dq, dk
     (summed over the heads of a group), dv, dg, dbeta (the inputs' dtype, contiguous) and, with
-    ``want_ds0``, ds0 (float32)."""
+    ``want_ds0``, ds0 (float32). ``operand_bits`` as for ``gated_delta_fwd``, for the states and the
+    gradients."""
     torch = _abi.torch()
+    operands = _operands(operand_bits)
     expanded = 0 in dy.stride()
     desc = describe_delta(q, k, v, g, beta, None if expanded else dy)
     for name, t in (("s0", s0), ("ds_final", ds_final)):
@@ -247,6 +249,7 @@ def gated_delta_bwd(q, k, v, g, beta, dy, scale: Optional[float] = None, *, s0=N
         if expanded:
             dy = dy.contiguous()
             desc = describe_delta(q, k, v, g, beta, dy)
+        desc.operands = operands
         need = gated_delta_bwd_workspace_size(desc)
         out = {n: torch.empty_like(t, memory_format=torch.contiguous_format) for n, t in
                (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))}

@@ -250,3 +250,9 @@ def test_delta_refuses_operands_that_do_not_exist(call):
     with pytest.raises(ValueError, match="operand_bits"):
         ins = make(2, 10, 4, 2, 16, 8, torch.float32)
         ssm.gated_delta_fwd(*[ins[n] for n in ("q", "k", "v", "g", "beta")], operand_bits=32)
+
+
+def test_backward_refuses_operand_bits_that_do_not_exist():
+    ins = make(2, 10, 4, 2, 16, 8, torch.float32)
+    with pytest.raises(ValueError, match="operand_bits"):
+        ssm.gated_delta_bwd(*[ins[n] for n in ("q", "k", "v", "g", "beta")], ins["v"], operand_bits=8)

@@ -8,7 +8,7 @@ results fit in 8 bits, so the tolerance is one rounding of bf16, 2^-8.
 """
 import pytest
 
-from delta_cases import make, reference, rel
+from delta_cases import double, make, reference, reference_grads, rel
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +179,192 @@ def test_sixteen_bits_by_choice(shape):
     y, S = ssm.gated_delta_fwd(*[ins[n] for n in NAMES], 0.3, s0=ins["s0"], final_state=True, operand_bits=16)
     assert rel(y, yr) <= 2.0 ** -8 + 2.0 ** -12
     assert rel(S, Sr) <= 4 * 2.0 ** -17
+
+
+# --- the backward pass ---------------------------------------------------------------------------
+# dy and ds_final beside the inputs; what is read back: a gradient's name and an index into it (after
+# the batch). P0 and P1 are two columns of v.
+P0, P1 = 0, 1
+
+
+def _blank_grads(L, dk):
+    ins = _blank(L, dk)
+    return dict(ins, dy=torch.zeros_like(ins["v"]), ds=torch.zeros_like(ins["s0"]))
+
+
+def _entries(dk):
+    """m 2^-23 along the entries of a key but the last two."""
+    m = torch.tensor(M) * 2.0 ** -23
+    return torch.cat([m.repeat(dk // len(M) + 1)[:dk - 2], torch.zeros(2)])
+
+
+def _read_state(dk):
+    """dq = S dY."""
+    ins = _blank_grads(2, dk)
+    ins["s0"][0, 0, P0] = 1 + D + _entries(dk)
+    ins["s0"][0, 0, P1] = 1 + D
+    ins["dy"][0, 1, 0, P0], ins["dy"][0, 1, 0, P1] = 1, -1
+    return ins, "dq", (1, 0, slice(0, dk - 2))
+
+
+def _write_of_the_state(dk):
+    """dv = beta dS k."""
+    ins = _blank_grads(2, dk)
+    ins["ds"][0, 0, :, 0] = 1 + D + _m()
+    ins["ds"][0, 0, :, 1] = 1 + D
+    _row(ins["k"], 0, _0=1, _1=-1)
+    ins["beta"][0, 0] = 1
+    return ins, "dv", (0, 0)
+
+
+def _key_of_the_state(dk):
+    """dk = dS u."""
+    ins = _blank_grads(2, dk)
+    ins["ds"][0, 0, P0] = 1 + D + _entries(dk)
+    ins["ds"][0, 0, P1] = 1 + D
+    ins["v"][0, 0, 0, P0], ins["v"][0, 0, 0, P1] = 1, -1
+    ins["beta"][0, 0] = 1
+    return ins, "dk", (0, 0, slice(0, dk - 2))
+
+
+def _key_of_the_correction(dk):
+    """dk = -S dr."""
+    ins = _blank_grads(2, dk)
+    ins["s0"][0, 0, P0] = 1 + D + _entries(dk)
+    ins["s0"][0, 0, P1] = 1 + D
+    ins["s0"][..., dk - 2:] = 0
+    ins["ds"][0, 0, P0, dk - 1], ins["ds"][0, 0, P1, dk - 1] = 1, -1
+    ins["k"][0, 0, 0, dk - 1] = 1
+    ins["beta"][0, 0] = 1
+    return ins, "dk", (0, 0, slice(0, dk - 2))
+
+
+def _read_writes(dk):
+    """dq = sum of E k: E of m 2^-23 from writes of 1 + 2^-10 + m 2^-23 and -(1 + 2^-10) in two columns."""
+    ins = _blank_grads(3, dk)
+    ins["s0"][0, 0, P0, 2], ins["s0"][0, 0, P1, 2] = -(D + 21 * 2.0 ** -23), D
+    _row(ins["k"], 0, _0=1, _2=1)
+    ins["beta"][0, 0] = 1
+    ins["v"][0, 0, 0, P0], ins["v"][0, 0, 0, P1] = 1, -1
+    ins["dy"][0, 2, 0, P0] = ins["dy"][0, 2, 0, P1] = 1
+    return ins, "dq", (2, 0, 0)
+
+
+def _weights_of_read_writes(dk):
+    """dq = sum of E k: E of 1 + 2^-10 + m 2^-23 and -(1 + 2^-10)."""
+    ins = _blank_grads(3, dk)
+    ins["s0"][0, 0, P0, 2], ins["s0"][0, 0, P0, 3] = -(D + 21 * 2.0 ** -23), D
+    _row(ins["k"], 0, _0=1, _1=1, _2=1)
+    _row(ins["k"], 1, _0=1, _1=-1, _3=1)
+    ins["beta"][0, :2] = 1
+    ins["v"][0, 0, 0, P0], ins["v"][0, 1, 0, P0] = 1, -1
+    ins["dy"][0, 2, 0, P0] = 1
+    return ins, "dq", (2, 0, 0)
+
+
+def _weights_of_reads(dk):
+    """dk = sum of E q."""
+    ins = _blank_grads(3, dk)
+    ins["s0"][0, 0, P0, 2], ins["s0"][0, 0, P1, 2] = -(D + 21 * 2.0 ** -23), -D
+    _row(ins["k"], 0, _2=1)
+    ins["beta"][0, 0] = 1
+    ins["v"][0, 0, 0, P0] = ins["v"][0, 0, 0, P1] = 1
+    _row(ins["q"], 1, _0=1, _1=1)
+    _row(ins["q"], 2, _0=1, _1=-1)
+    ins["dy"][0, 1, 0, P0], ins["dy"][0, 2, 0, P1] = 1, -1
+    return ins, "dk", (0, 0, 0)
+
+
+def _weights_of_corrections(dk):
+    """dk = sum of M k."""
+    ins = _blank_grads(3, dk)
+    ins["s0"][0, 0, P0, 2], ins["s0"][0, 0, P1, 2] = -(D + 21 * 2.0 ** -23), -D
+    _row(ins["k"], 0, _2=1)
+    _row(ins["k"], 1, _0=1, _1=1, _4=1)
+    _row(ins["k"], 2, _0=1, _1=-1, _5=1)
+    ins["beta"][0] = 1
+    ins["v"][0, 0, 0, P0] = ins["v"][0, 0, 0, P1] = 1
+    ins["ds"][0, 0, P0, 4], ins["ds"][0, 0, P1, 5] = -1, 1
+    return ins, "dk", (0, 0, 0)
+
+
+def _strength(dk):
+    """dbeta = dr.v."""
+    ins = _blank_grads(2, dk)
+    ins["ds"][0, 0, P0, 0], ins["ds"][0, 0, P1, 0] = 1 + D + 21 * 2.0 ** -23, -(1 + D)
+    _row(ins["k"], 0, _0=1)
+    ins["beta"][0, 0] = 1
+    ins["v"][0, 0, 0, P0] = ins["v"][0, 0, 0, P1] = 1
+    return ins, "dbeta", (0, 0)
+
+
+def _decay(dk):
+    """dg = <S, dS>."""
+    ins = _blank_grads(2, dk)
+    ins["s0"][0, 0, P0, 0], ins["s0"][0, 0, P1, 0] = 1 + D + 21 * 2.0 ** -23, 1 + D
+    ins["ds"][0, 0, P0, 0], ins["ds"][0, 0, P1, 0] = 1, -1
+    return ins, "dg", (0, 0)
+
+
+def _passed_back(dk, L=200, at=150):
+    """dS <- dS - k dr, read chunks before: dr of 1 + 2^-10 + m 2^-23 beside an entry of 1 + 2^-10."""
+    ins = _blank_grads(L, dk)
+    ins["ds"][0, 0, :, 0], ins["ds"][0, 0, :, 1] = 1 + D, _m()
+    _row(ins["k"], at, _0=1, _1=1)
+    _row(ins["k"], 0, _0=1)
+    ins["beta"][0, 0] = ins["beta"][0, at] = 1
+    return ins, "dv", (0, 0)
+
+
+def _passed_back_over_segments(dk):
+    return _passed_back(dk, 1500, 1400)
+
+
+GRAD_CASES = [_read_state, _write_of_the_state, _key_of_the_state, _key_of_the_correction, _read_writes,
+              _weights_of_read_writes, _weights_of_reads, _weights_of_corrections, _strength, _decay,
+              _passed_back, _passed_back_over_segments]
+
+
+@pytest.mark.parametrize("dk", [24, 64, 128])
+@pytest.mark.parametrize("case", GRAD_CASES, ids=lambda f: f.__name__[1:])
+def test_backward_carries_24_bits(case, dk):
+    import selective_state_space_24_amd as ssm
+    ins, name, at = case(dk)
+    wide = {n: ins[n].double() for n in NAMES + ("s0",)}
+    want = reference_grads(wide, 1.0, ins["dy"].double(), ins["ds"].double())[name][(0,) + at]
+    assert want.abs().min() > 0 and torch.equal(want.to(BF16).double(), want)
+    dev, s0 = _inputs(ins)
+    dy, ds = ins["dy"].to(BF16).cuda(), ins["ds"].cuda()
+    for ds0 in (False, True):
+        got = ssm.gated_delta_bwd(*[dev[n] for n in NAMES], dy, 1.0, s0=s0, ds_final=ds, want_ds0=ds0)
+        assert rel(got[name][(0,) + at], want) <= ONE
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("bits", [24, 16])
+def test_gradients_do_not_depend_on_the_states_being_asked_for(shape, bits):
+    import selective_state_space_24_amd as ssm
+    ins = {n: t.cuda() for n, t in make(*shape, BF16, seed=5, s0=True).items()}
+    a = [ins[n] for n in NAMES]
+    dy = torch.randn(ins["v"].shape, device="cuda", generator=torch.Generator("cuda").manual_seed(6)).to(BF16)
+    one = ssm.gated_delta_bwd(*a, dy, 0.3, s0=ins["s0"], operand_bits=bits)
+    two = ssm.gated_delta_bwd(*a, dy, 0.3, s0=ins["s0"], want_ds0=True, operand_bits=bits)
+    assert all(torch.equal(one[n], two[n]) for n in one)
+
+
+@pytest.mark.parametrize("shape", SHAPES[:2] + SHAPES[3:], ids=lambda s: "-".join(map(str, s)))
+def test_sixteen_bits_by_choice_in_the_backward_pass(shape):
+    """One rounding to 8 bits and 2^-12 before it, 8 times that for dg, a sum over the later steps of a
+    chunk; ds0 as the state in the forward pass."""
+    import selective_state_space_24_amd as ssm
+    cpu = make(*shape, BF16, seed=7, s0=True)
+    ins = {n: t.cuda() for n, t in cpu.items()}
+    gen = torch.Generator().manual_seed(8)
+    dy = torch.randn(cpu["v"].shape, generator=gen).to(BF16)
+    ds = torch.randn(cpu["s0"].shape, generator=gen)
+    want = reference_grads(double(cpu), 0.3, dy.double(), ds.double())
+    got = ssm.gated_delta_bwd(*[ins[n] for n in NAMES], dy.cuda(), 0.3, s0=ins["s0"], ds_final=ds.cuda(),
+                              want_ds0=True, operand_bits=16)
+    for n in want:
+        bound = 4 * 2.0 ** -17 if n == "ds0" else 2.0 ** -8 + (8 if n == "dg" else 1) * 2.0 ** -12
+        assert rel(got[n], want[n]) <= bound, n

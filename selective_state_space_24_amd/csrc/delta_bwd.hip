@@ -11,9 +11,9 @@
 //      dK_s = sum_{t >= s} scale D_ts E_ts Q_t + sum_x M_xs K_x - beta_s e^{G_s} S dR_s
 //             + e^{G_63 - G_s} dS U_s,    M_ts = M_st = beta_t D_ts N_ts (s < t)
 //      dbeta_t = dR_t . V_t - e^{G_t} K_t . (S dR_t) + sum_{s < t} N_ts D_ts K_t . K_s
-//      dG_x = sum_s (E.P + N.A)_xs - sum_t (E.P + N.A)_tx + Q_x . (scale e^{G_x} S dY_x)
+//      dG_x = sum_{s < x} (E.P + N.A)_xs - sum_{t > x} (E.P + N.A)_tx + Q_x . (scale e^{G_x} S dY_x)
 //             - K_x . (beta_x e^{G_x} S dR_x) - K_x . (e^{G_63 - G_x} dS U_x)
-//             (at 63: + sum_s K_s . (e^{G_63 - G_s} dS U_s) + e^{G_63} <S, dS>)
+//             (at 63 instead of the last: + sum_{s < 63} K_s . (e^{G_63 - G_s} dS U_s) + e^{G_63} <S, dS>)
 //      dg_t = sum_{x >= t} dG_x
 #include "delta_common.h"
 
@@ -589,7 +589,9 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
           const int x = tile_row4(a, 0) + i;
           const float w1 = x <= on ? p.scale * d[i] * m1[a][i] : 0.0f;
           const float w2 = x >= yx && x < nx ? p.scale * d[i] * m2[a][i] : 0.0f;
-          dG += w1 * k4[i] - w2 * q4[i];
+          // step y itself is in the rows' sum and the columns': neither, else the two products' roundings,
+          // which no decay makes small, stay in dG
+          dG += x == yx ? 0.0f : w1 * k4[i] - w2 * q4[i];
           m1[a][i] = w1;
           m2[a][i] = w2;
         }
@@ -641,6 +643,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
       }
     }
     dbe = sum_groups(dbe + kr + rv);
+    ku = y < n - 1 ? ku : 0.0f;  // the last step's, without decay, is taken away and added again
     dG = sum_groups(dG + qs + by * kr - ku);
     ku = sum_groups(ku);
     ss = sum_groups(ss);
@@ -649,7 +652,7 @@ __global__ void __launch_bounds__(512) delta_grad_kernel(const DeltaBwdParams q)
     if (g == 0) {
       *sums(part * kC + y) = dG;
       *sums((2 + part) * kC + y) = dbe;
-      *sums((4 + part) * kC + y) = y < n ? ku : 0.0f;
+      *sums((4 + part) * kC + y) = ku;
     }
     if (lane == 0) *sums(6 * kC + wave) = ss;
     sync_lds();

@@ -23,6 +23,9 @@
  *
  * Steps are taken in chunks of 64 as matrix products: a NaN or an infinity in an input reaches,
  * beside the steps from its own on, the other steps of its chunk.
+ *
+ * Sizes that would take 2^32 threads in a launch (about 2^23 heads, or chunks of one group) return
+ * SSM_ERR_UNSUPPORTED.
  */
 #ifndef SSM_DELTA_H
 #define SSM_DELTA_H

@@ -15,7 +15,7 @@ using ssm::aligned;
 using ssm::Buf;
 using ssm::check_buffers;
 
-constexpr int64_t kMaxGrid = 0x7fffffff;  // workgroups of a launch
+constexpr int64_t kMaxThreads = 0xffffffff;  // of a launch, along one dimension
 
 // A tensor of up to three outer dimensions and an innermost one of stride 1.
 struct Shape {
@@ -206,6 +206,13 @@ BwdLayout bwd_layout(const ssm_delta_desc& d) {
   return l;
 }
 
+// Every launch of a pass that is not split (a split one has few heads) has a 32-bit number of threads.
+bool launchable(const ssm::DeltaParams& p, bool bwd) {
+  const int64_t heads = p.batch * p.nheads, columns = 16 * ssm::delta_scan_waves(p);
+  return p.nchunks <= kMaxThreads / 256 && heads * ((p.dv + columns - 1) / columns) <= kMaxThreads / (4 * columns) &&
+         (!bwd || p.batch * p.ngroups * p.nchunks <= kMaxThreads / 512);
+}
+
 int run_status(hipError_t e) { return e == hipSuccess ? SSM_OK : SSM_ERR_HIP; }
 
 }  // namespace
@@ -261,10 +268,9 @@ int ssm_gated_delta_fwd(const ssm_delta_desc* desc, const void* q, const void* k
   if (rc != SSM_OK) return rc;
   if (!steps)
     return s_final ? run_status(ssm::launch_state_copy(s0, s_final, (int64_t)(sb / 4), hs)) : SSM_OK;
-  if (d.batch * d.nheads * chunks(d) > kMaxGrid || d.batch * d.nheads * ((d.headdim + 63) / 64) > kMaxGrid)
-    return SSM_ERR_UNSUPPORTED;
   ssm::DeltaParams p;
   fill(d, q, k, v, g, beta, scale, &p);
+  if (!launchable(p, false)) return SSM_ERR_UNSUPPORTED;
   p.y = y; p.s0 = s0; p.s_final = s_final;
   // (row_access asks more of y than its 8-byte stores need)
   p.vec_y = row_access(d, d.headdim, y, shape_y(d).s);
@@ -296,7 +302,8 @@ int ssm_gated_delta_update(const ssm_delta_desc* desc, float* state, const void*
   const Buf out[] = {{y, extent(shape_y(d)) * es, es}, {state, state_bytes(d), 4}};
   rc = check_buffers(in, 5, out, 2);
   if (rc != SSM_OK) return rc;
-  if (d.batch * d.nheads * ((d.headdim + 7) / 8) > kMaxGrid) return SSM_ERR_UNSUPPORTED;
+  // (with more heads than that, a wavefront takes 32 rows)
+  if (d.batch * d.nheads * ((d.headdim + 31) / 32) > kMaxThreads / 256 * 4) return SSM_ERR_UNSUPPORTED;
   ssm::DeltaParams p;
   fill(d, q, k, v, g, beta, scale, &p);
   p.y = y;
@@ -344,11 +351,10 @@ int ssm_gated_delta_bwd(const ssm_delta_desc* desc, const void* q, const void* k
   if (rc != SSM_OK) return rc;
   if (!steps)
     return ds0 ? run_status(ssm::launch_state_copy(ds_final, ds0, (int64_t)(sb / 4), hs)) : SSM_OK;
-  if (d.batch * d.nheads * chunks(d) > kMaxGrid || d.batch * d.nheads * ((d.headdim + 63) / 64) > kMaxGrid)
-    return SSM_ERR_UNSUPPORTED;
   ssm::DeltaBwdParams p;
   memset(&p, 0, sizeof(p));
   fill(d, q, k, v, g, beta, scale, &p.f);
+  if (!launchable(p.f, true)) return SSM_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.f.s0 = s0;
   p.f.rec = ws; p.f.image = ws + lay.image; p.image_b = ws + lay.image_b;

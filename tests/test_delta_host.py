@@ -256,3 +256,20 @@ def test_backward_refuses_operand_bits_that_do_not_exist():
     ins = make(2, 10, 4, 2, 16, 8, torch.float32)
     with pytest.raises(ValueError, match="operand_bits"):
         ssm.gated_delta_bwd(*[ins[n] for n in ("q", "k", "v", "g", "beta")], ins["v"], operand_bits=8)
+
+
+def test_delta_refuses_launches_past_32_bits_of_threads():
+    """A launch's threads along a dimension are a 32-bit number: 2^24 workgroups of 512, 2^26 of 64."""
+    names = ("q", "k", "v", "g", "beta", "y", "dy", "dq", "dk", "dv", "dg", "dbeta", "ws", "state")
+    room = {n: (i + 1) << 50 for i, n in enumerate(names)}
+    inputs = {n: room[n] for n in DELTA_IN}
+    grads = {n: room[n] for n in ("dy", "dq", "dk", "dv", "dg", "dbeta")}
+    d = ssm.delta_desc_contiguous(1 << 12, 1, 1 << 12, 1 << 12, 1, 65)  # 2^24 heads, eight wavefronts each
+    assert _fwd(d, y=room["y"], ws=room["ws"], wsb=1 << 62, **inputs) == -9
+    assert _bwd(d, ws=room["ws"], wsb=1 << 62, **grads, **inputs) == -9
+    d = ssm.delta_desc_contiguous(1 << 12, 1, 1 << 11, 1 << 11, 1, 1)  # scans of half as many; gradients not
+    assert _bwd(d, ws=room["ws"], wsb=1 << 62, **grads, **inputs) == -9
+    d = ssm.delta_desc_contiguous(1, (1 << 30) + 1, 1, 1, 1, 1)  # 2^24 chunks and one
+    assert _fwd(d, y=room["y"], ws=room["ws"], wsb=1 << 62, **inputs) == -9
+    d = ssm.delta_desc_contiguous(1 << 14, 1, 1 << 13, 1 << 13, 1, 1)
+    assert ssm.gated_delta_update_raw(d, room["state"], *[room[n] for n in DELTA_IN], 0.1, room["y"], None) == -9

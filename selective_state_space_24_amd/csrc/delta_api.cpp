@@ -73,7 +73,9 @@ int check_desc(const ssm_delta_desc* d) {
   if (d->batch < 0 || d->seqlen < 0 || d->nheads < 1 || d->ngroups < 1 || d->nheads % d->ngroups ||
       d->dstate < 1 || d->dstate > SSM_DELTA_MAX_DSTATE || d->headdim < 1)
     return SSM_ERR_BAD_SHAPE;
-  int64_t t = 512, u;  // room for every buffer of the passes, in bytes
+  // room for every buffer of the passes, in bytes: a step of one head of one entry each way takes up
+  // to 1400 (records 608, images 384, copies 320, a split's matrices 48)
+  int64_t t = 4096, u;
   for (int64_t n : {d->batch, d->nheads, d->headdim, d->dstate})
     if (__builtin_mul_overflow(t, n > 0 ? n : 1, &t)) return SSM_ERR_BAD_SHAPE;
   if (__builtin_mul_overflow(t, d->seqlen + 64, &u)) return SSM_ERR_BAD_SHAPE;

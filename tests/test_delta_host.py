@@ -273,3 +273,16 @@ def test_delta_refuses_launches_past_32_bits_of_threads():
     assert _fwd(d, y=room["y"], ws=room["ws"], wsb=1 << 62, **inputs) == -9
     d = ssm.delta_desc_contiguous(1 << 14, 1, 1 << 13, 1 << 13, 1, 1)
     assert ssm.gated_delta_update_raw(d, room["state"], *[room[n] for n in DELTA_IN], 0.1, room["y"], None) == -9
+
+
+@pytest.mark.parametrize("seqlen", [1 << 40, 1 << 50, (1 << 54) - 65, (1 << 54) + 64, 1 << 55])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_delta_workspace_sizes_do_not_wrap(seqlen, dtype):
+    """Either the size that is needed (the records of the chunks alone take over 200 bytes a step) or a
+    refusal."""
+    d = ssm.delta_desc_contiguous(1, seqlen, 1, 1, 1, 1, dtype)
+    for size in (ssm.gated_delta_workspace_size, ssm.gated_delta_bwd_workspace_size):
+        try:
+            assert size(d) >= 200 * seqlen
+        except ssm.ScanError as e:
+            assert e.status == -2

@@ -97,10 +97,10 @@ def gated_delta_bwd_raw(desc, q, k, v, g, beta, scale, s0, dy, ds_final, dq, dk,
 # ---------------------------------------------------------------------------------------------
 # torch front end
 
-def _check_like(v, keys, values, steps, q, k, g, beta, y):
+def _check_like(v, keys, values, steps, q, k, g, beta, y, y_name):
     """Raises for the first tensor that has not v's dtype and device and its shape."""
     for name, t, shape in (("q", q, keys), ("k", k, keys), ("g", g, steps), ("beta", beta, steps),
-                           ("y", y, values)):
+                           (y_name, y, values)):
         if t is None:
             continue
         if t.dtype != v.dtype:
@@ -125,8 +125,9 @@ def _unit(name, st, n):
         raise ValueError(f"{name} must have unit stride along its last dimension")
 
 
-def describe_delta(q, k, v, g, beta, y=None) -> DeltaDesc:
-    """Descriptor of torch tensors (shapes as in the module's docstring)."""
+def describe_delta(q, k, v, g, beta, y=None, y_name: str = "y") -> DeltaDesc:
+    """Descriptor of torch tensors (shapes as in the module's docstring); ``y_name`` is what an error
+    calls y."""
     if v.dim() != 4 or q.dim() != 4:
         raise ValueError("expected q, k (batch, L, ngroups, dstate) and v (batch, L, nheads, headdim)")
     batch, L, nheads, dv = values = v.shape
@@ -134,17 +135,17 @@ def describe_delta(q, k, v, g, beta, y=None) -> DeltaDesc:
     io = _abi.io_dtype("v", v)
     keys, steps = (batch, L, groups, dk), (batch, L, nheads)
     if y is not None or not _alike(v, keys, steps, q, k, g, beta):
-        _check_like(v, keys, values, steps, q, k, g, beta, y)
+        _check_like(v, keys, values, steps, q, k, g, beta, y, y_name)
     qs, ks, vs = q.stride(), k.stride(), v.stride()
     ys = y.stride() if y is not None else (L * nheads * dv, nheads * dv, dv, 1)
     if qs[3] != 1 or ks[3] != 1 or vs[3] != 1 or ys[3] != 1:
-        for name, st, n in (("q", qs, dk), ("k", ks, dk), ("v", vs, dv), ("y", ys, dv)):
+        for name, st, n in (("q", qs, dk), ("k", ks, dk), ("v", vs, dv), (y_name, ys, dv)):
             _unit(name, st, n)
     return DeltaDesc(batch, L, nheads, groups, dk, dv, io, 0, *qs[:3], *ks[:3], *vs[:3],
                      *g.stride(), *beta.stride(), *ys[:3])
 
 
-def describe_delta_step(q, k, v, g, beta, y=None) -> DeltaDesc:
+def describe_delta_step(q, k, v, g, beta, y=None, y_name: str = "y") -> DeltaDesc:
     """Descriptor (seqlen 1) of one step: q, k (batch, ngroups, dstate), v, y (batch, nheads,
     headdim), g, beta (batch, nheads)."""
     if v.dim() != 3 or q.dim() != 3:
@@ -154,11 +155,11 @@ def describe_delta_step(q, k, v, g, beta, y=None) -> DeltaDesc:
     io = _abi.io_dtype("v", v)
     keys, steps = (batch, groups, dk), (batch, nheads)
     if y is not None or not _alike(v, keys, steps, q, k, g, beta):
-        _check_like(v, keys, values, steps, q, k, g, beta, y)
+        _check_like(v, keys, values, steps, q, k, g, beta, y, y_name)
     (qb, qg, q1), (kb, kg, k1), (vb, vh, v1) = q.stride(), k.stride(), v.stride()
     yb, yh, y1 = y.stride() if y is not None else (nheads * dv, dv, 1)
     if q1 != 1 or k1 != 1 or v1 != 1 or y1 != 1:
-        for name, st, n in (("q", (q1,), dk), ("k", (k1,), dk), ("v", (v1,), dv), ("y", (y1,), dv)):
+        for name, st, n in (("q", (q1,), dk), ("k", (k1,), dk), ("v", (v1,), dv), (y_name, (y1,), dv)):
             _unit(name, st, n)
     gb, gh = g.stride()
     bb, bh = beta.stride()
@@ -193,7 +194,7 @@ def gated_delta_fwd(q, k, v, g, beta, scale: Optional[float] = None, *, s0=None,
     defaults to the current torch stream. Raises ScanError with the library's status on failure.
     """
     torch = _abi.torch()
-    desc = describe_delta(q, k, v, g, beta, out)
+    desc = describe_delta(q, k, v, g, beta, out, "out")
     desc.operands = _operands(operand_bits)
     if s0 is not None:
         _check_state("s0", s0, desc, v.device)
@@ -220,7 +221,7 @@ def gated_delta_update(state, q, k, v, g, beta, scale: Optional[float] = None, *
     """One step per batch entry: updates ``state`` in place and returns y (batch, nheads, headdim).
     q, k are (batch, ngroups, dstate), v (batch, nheads, headdim), g and beta (batch, nheads)."""
     torch = _abi.torch()
-    desc = describe_delta_step(q, k, v, g, beta, out)
+    desc = describe_delta_step(q, k, v, g, beta, out, "out")
     _check_state("state", state, desc, v.device)
     with _abi.launch(v, stream) as sp:
         y = out if out is not None else torch.empty_like(v, memory_format=torch.contiguous_format)
@@ -241,14 +242,14 @@ def gated_delta_bwd(q, k, v, g, beta, dy, scale: Optional[float] = None, *, s0=N
     torch = _abi.torch()
     operands = _operands(operand_bits)
     expanded = 0 in dy.stride()
-    desc = describe_delta(q, k, v, g, beta, None if expanded else dy)
+    desc = describe_delta(q, k, v, g, beta, None if expanded else dy, "dy")
     for name, t in (("s0", s0), ("ds_final", ds_final)):
         if t is not None:
             _check_state(name, t, desc, v.device)
     with _abi.launch(v, stream) as sp:
         if expanded:
             dy = dy.contiguous()
-            desc = describe_delta(q, k, v, g, beta, dy)
+            desc = describe_delta(q, k, v, g, beta, dy, "dy")
         desc.operands = operands
         need = gated_delta_bwd_workspace_size(desc)
         out = {n: torch.empty_like(t, memory_format=torch.contiguous_format) for n, t in

@@ -286,3 +286,23 @@ def test_delta_workspace_sizes_do_not_wrap(seqlen, dtype):
             assert size(d) >= 200 * seqlen
         except ssm.ScanError as e:
             assert e.status == -2
+
+
+def test_python_names_the_tensor_that_does_not_fit():
+    ins = make(2, 10, 4, 2, 16, 8, torch.float32)
+    args = [ins[n] for n in ("q", "k", "v", "g", "beta")]
+    v = ins["v"]
+    wide = torch.empty(2, 10, 4, 16)[..., ::2]
+    with pytest.raises(TypeError, match="^dy has dtype"):
+        ssm.gated_delta_bwd(*args, v.bfloat16())
+    with pytest.raises(ValueError, match="^dy must be"):
+        ssm.gated_delta_bwd(*args, v[:, :9])
+    with pytest.raises(ValueError, match="^dy must have unit stride"):
+        ssm.gated_delta_bwd(*args, wide)
+    with pytest.raises(TypeError, match="^out has dtype"):
+        ssm.gated_delta_fwd(*args, out=v.bfloat16())
+    with pytest.raises(ValueError, match="^out must have unit stride"):
+        ssm.gated_delta_fwd(*args, out=wide)
+    one = [t[:, 0] for t in args]
+    with pytest.raises(ValueError, match="^out must be"):
+        ssm.gated_delta_update(torch.zeros(2, 4, 8, 16), *one, out=v[:, 0, :, :4])

@@ -37,9 +37,11 @@ struct BackLds {
   static constexpr int kAll = kBuf.n * kBytes + kBuf.tiles * Move::kTileBytes;
 };
 
-// Four products to the forward scan's five, with T and P transposed on the way out of LDS: 760 us for
+// Four products to the forward scan's five, with T and P transposed on the way out of LDS: 740 us for
 // batch 4, 8192 steps of 64 heads, 128 x 64 in bf16 (680 with 16-bit operands), of which 1.6 GB of
-// image written take 330 us at a copy's rate.
+// image written take 330 us at a copy's rate. There 256 workgroups of four wavefronts leave one to a
+// SIMD, which spends 27 % of the time in matrix and 24 % in other vector instructions; the LDS is busy
+// 43 % of it, 29 % with the bank conflicts of the transposed reads.
 //
 // dV leaves a chunk late, as the forward scan's y does. Where the sequence is split, a first run
 // (LOCAL) makes what each segment but the first adds to the gradient of the state before it, from
@@ -317,7 +319,8 @@ __global__ void __launch_bounds__(64 * NW) delta_back_kernel(const DeltaBwdParam
 //
 // Bound by latency within the CU: the LDS (153 KB with keys of 128, three terms; 145 KB with two)
 // leaves room for one workgroup on each. Batch 4, 8192 steps of 64 heads (16 of keys), 128 x 64 in
-// bf16: 1.94 ms, with 16-bit operands 1.4 ms (5 % less if the same slice is read every time).
+// bf16: 1.8-1.9 ms, with 16-bit operands 1.4 ms (5 % less if the same slice is read every time).
+// The SIMDs spend 27 % of the time in matrix and 37 % in other vector instructions.
 template <class P, int KK>
 struct GradLds {
   typedef Image<P, KK> Img;

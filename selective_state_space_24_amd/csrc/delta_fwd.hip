@@ -19,8 +19,9 @@ namespace {
 // Substitution and fp32 blocks: a product form of the inverse in powers of A loses digits where
 // keys repeat. G is summed in fp64: e^{G_t - G_s} of two large sums keeps its digits.
 //
-// Bound by instruction issue: 190 us for 16384 chunks with keys of 128 in bf16, which write 0.41 GB
-// of records (85 us at the rate of a copy) and read 0.27 GB.
+// Near the memory's rate: 212 us for 16384 chunks with keys of 128 in bf16, which write 0.62 GB of
+// records and read 0.27 GB (4.2 TB/s; a large copy 4.8). The SIMDs spend 12 % of the time in matrix and
+// 38 % in other vector instructions, wavefronts 58 % of theirs waiting for memory or each other.
 constexpr int kAtStride = kC + 4;  // floats per row of A^T in LDS
 
 // inclusive prefix sum over the 64 lanes, in fp64, by DPP moves (see wave_inclusive_sum's steps in
@@ -204,9 +205,10 @@ __global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaParams p) {
 // chunk: where two buffers have room for one tile of v only, the next chunk's is loaded behind a
 // barrier in the middle of the chunk.
 //
-// Bound by the wavefronts' own matrix and vector instructions, which overlap little at the two
-// wavefronts a SIMD that the registers allow: batch 8, 4096 steps of 32 heads, 128 x 128 in bf16
-// takes 310 us, and 9 % less if every chunk reads the same memory.
+// Bound by the wavefronts' own matrix and vector instructions (54 and 40 % of the SIMDs' time), which
+// overlap little at the two wavefronts a SIMD that the registers allow: batch 8, 4096 steps of 32
+// heads, 128 x 128 in bf16 takes 440 us; with 16-bit operands 310, and 9 % less if every chunk reads
+// the same memory.
 //
 // kStates, the backward pass's first scan: no y; the state before each chunk and U go to the image.
 //
@@ -741,8 +743,10 @@ size_t delta_image_bytes(int64_t dk, int64_t dv) {
 }
 
 // Columns per workgroup: as many as leave a workgroup for every CU (a wider one reads K, Q, T and
-// P once for more columns). 4096 steps of keys of 128 in bf16, at 64 and at 128 columns: 256 heads
-// of 128 474 and 383 us; 128 heads of 128 226 and 285 us.
+// P once for more columns). 4096 steps of keys of 128 in bf16, the whole call, at 64 and at 128
+// columns: 256 heads of 128 770 and 685 us; 128 heads of 128 376 and 462 us; 64 heads of 256 315 and
+// 410 us. In fp32 the wide scan with keys of 128 spills seven registers and is the faster all the same
+// (256 heads of 128 1.88 and 1.64 ms).
 int delta_scan_waves(const DeltaParams& p) {
   const int64_t tiles = (p.dv + 15) / 16;
   return tiles > 4 && p.batch * p.nheads * ((tiles + 7) / 8) * p.nseg >= kCUs ? 8 : 4;
@@ -751,9 +755,9 @@ int delta_scan_waves(const DeltaParams& p) {
 // In steps of one chunk of a workgroup of 128 columns: a whole sequence takes nchunks, a split one
 // its summary pass, its scan, up to one for each segment in the combine kernel (less with short
 // keys, and as fp32 chunks take longer), and three for the two launches. Split where that is a fifth
-// less. All kernels together, whole and split: 2 x 8 heads of 64 x 64 in fp32, 16 chunks 108 and 59
-// us; 128 x 128 in bf16, 16 heads of 1024 chunks 2924 and 1169 us, of 64 chunks 187 and 110 us, 32
-// heads of 32 chunks 106 and 96 us. The backward pass takes both scans twice, and its own combine
+// less. The call, whole and split: 2 x 8 heads of 64 x 64 in fp32, 16 chunks 111 and 59 us; 128 x 128
+// in bf16, 16 heads of 1024 chunks 4109 and 1250 us, of 64 chunks 266 and 145 us, 32 heads of 64
+// chunks 277 and 190 us, of 32 chunks 144 and 125 us (16 heads of 16 chunks are left whole: 78 us). The backward pass takes both scans twice, and its own combine
 // run, for two whole ones: the same comparison.
 void delta_plan(DeltaParams* p) {
   p->nseg = 1;

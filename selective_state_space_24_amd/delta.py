@@ -2,7 +2,8 @@
 
 Tensors: q, k (batch, L, ngroups, dstate); v, y (batch, L, nheads, headdim); g, beta
 (batch, L, nheads), all bfloat16 or all float32, any strides with a unit innermost one. States are
-(batch, nheads, headdim, dstate) float32, contiguous.
+(batch, nheads, headdim, dstate) float32, contiguous. As with the scan, the calls record no autograd
+graph: ``gated_delta_bwd`` is called for the gradients.
 """
 from __future__ import annotations
 

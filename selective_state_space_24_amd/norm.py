@@ -1,7 +1,8 @@
 """Python binding of layer norm (``include/ssm_norm.h``): argument marshalling only.
 
 x, y and their gradients are bfloat16 or float32 tensors of any number of dimensions, normalised
-over the last; weight, bias, the statistics and the parameter gradients are float32.
+over the last; weight, bias, the statistics and the parameter gradients are float32. As with the scan,
+the calls record no autograd graph: ``layer_norm_bwd`` is called for the gradients.
 """
 from __future__ import annotations
 
